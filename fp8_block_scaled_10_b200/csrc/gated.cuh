@@ -81,8 +81,8 @@ __global__ void __launch_bounds__(256) gated_reduce_kernel(const ReduceParams p)
     float g[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
     for (int sp = 0; sp < p.splits; ++sp) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(base + sp * step));
-      const float4 b = __ldg(reinterpret_cast<const float4*>(base + sp * step + up));
+      const float4 a = __ldcg(reinterpret_cast<const float4*>(base + sp * step));
+      const float4 b = __ldcg(reinterpret_cast<const float4*>(base + sp * step + up));
       g[0] += a.x; g[1] += a.y; g[2] += a.z; g[3] += a.w;
       u[0] += b.x; u[1] += b.y; u[2] += b.z; u[3] += b.w;
     }
@@ -238,9 +238,9 @@ __global__ void __launch_bounds__(256)
     for (int j = 0; j < 8; ++j) {
       g[j] = u[j] = d[j] = __nv_bfloat16(0.0f);
       if (col + 256 * j < N) {
-        g[j] = gp[256 * j];
-        u[j] = gp[N + 256 * j];
-        d[j] = dhp[256 * j];
+        g[j] = __ldcs(gp + 256 * j);
+        u[j] = __ldcs(gp + N + 256 * j);
+        d[j] = __ldcs(dhp + 256 * j);
       }
     }
     __nv_bfloat16* dp = dgu + row * 2 * N + col;

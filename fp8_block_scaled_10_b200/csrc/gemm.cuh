@@ -346,7 +346,7 @@ __device__ __forceinline__ void group_table(const Params& p, int* table, int lan
                                             int* num_units) {
   int* row_off = table + kMaxGroups + 1;
   for (int g = lane; g <= p.groups; g += 32) {
-    int64_t o = __ldg(p.m_offsets + g);
+    int64_t o = __ldca(p.m_offsets + g);
     o = o < 0 ? 0 : (o > p.M ? p.M : o);
     row_off[g] = static_cast<int>(o);
   }
@@ -864,7 +864,7 @@ __global__ void __launch_bounds__(Cfg<BN, ARows>::kThreads, 1)
         for (int j = 0; j < 4; ++j) {
           const int64_t row = c.row0 + lane + 32 * j;
           va[j] = (c.valid && row < c.row_end)
-                      ? __ldg(BROW ? p.sa + c.kb * p.M + row : p.sa + row * p.kbn + c.kb)
+                      ? p.sa[BROW ? c.kb * p.M + row : row * p.kbn + c.kb]
                       : 0.0f;
         }
       }
@@ -874,18 +874,17 @@ __global__ void __launch_bounds__(Cfg<BN, ARows>::kThreads, 1)
 #pragma unroll
         for (int j = 0; j < kWRegs; ++j) {
           const int64_t col = c.n0 + lane + 32 * j;
-          vw[j] = (c.valid && col < p.N) ? __ldg(p.sw + c.kb * static_cast<int64_t>(p.N) + col) : 0.0f;
+          vw[j] = (c.valid && col < p.N) ? p.sw[c.kb * static_cast<int64_t>(p.N) + col] : 0.0f;
         }
       } else if (GATED) {
         // lane 0: the gate block's scale, lane 1: the up block's
         vw[0] = (c.valid && lane < 2)
-                    ? __ldg((lane ? p.sw_up : p.sw) +
-                            (static_cast<int64_t>(c.group) * p.nbn + c.nb0) * p.kbn + c.kb)
+                    ? (lane ? p.sw_up : p.sw)[(static_cast<int64_t>(c.group) * p.nbn + c.nb0) * p.kbn + c.kb]
                     : 0.0f;
       } else {
         const int nb = c.nb0 + lane;
         vw[0] = (c.valid && lane < kNbPerTile && nb < p.nbn)
-                    ? __ldg(p.sw + (static_cast<int64_t>(c.group) * p.nbn + nb) * p.kbn + c.kb)
+                    ? p.sw[(static_cast<int64_t>(c.group) * p.nbn + nb) * p.kbn + c.kb]
                     : 0.0f;
       }
     };
@@ -973,7 +972,7 @@ __global__ void __launch_bounds__(Cfg<BN, ARows>::kThreads, 1)
       for (int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + lane; i < na; i += 4 * step_a) {
         float v[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = i + j * step_a < na ? __ldg(p.sa + i + j * step_a) : 1.0f;
+        for (int j = 0; j < 4; ++j) v[j] = i + j * step_a < na ? __ldca(p.sa + i + j * step_a) : 1.0f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) bad |= not_pow2(v[j]);
       }
@@ -989,7 +988,7 @@ __global__ void __launch_bounds__(Cfg<BN, ARows>::kThreads, 1)
             const int el = i + 32 * j;
             const int nb = nb0 + el / nkb;
             v[j] = (el < cnt && nb < p.nbn)
-                       ? __ldg(p.sw + static_cast<int64_t>(nb) * p.kbn + t.kb0 + el % nkb)
+                       ? __ldca(p.sw + static_cast<int64_t>(nb) * p.kbn + t.kb0 + el % nkb)
                        : 1.0f;
           }
 #pragma unroll
@@ -1308,7 +1307,7 @@ __global__ void __launch_bounds__(256)
     if (row >= M || col >= N) continue;
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int sp = 0; sp < splits; ++sp) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(
           ws + ((static_cast<int64_t>(tt) * splits + sp) * BM + r) * bn + c));
       s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
     }

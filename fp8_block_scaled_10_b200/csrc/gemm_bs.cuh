@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(BsCfg<BN>::kThreads, 1)
           const int64_t rc = rin[r] ? row : t.row_end - 1;
 #pragma unroll
           for (int j = 0; j < kG; ++j)
-            va[r][j] = __ldg(BROW ? p.sa + static_cast<int64_t>(kbc[j]) * p.M + rc
+            va[r][j] = __ldca(BROW ? p.sa + static_cast<int64_t>(kbc[j]) * p.M + rc
                                   : p.sa + rc * p.kbn + kbc[j]);
         }
         constexpr int kWR = BROW ? 4 : 1;   // W rows per lane and atom
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(BsCfg<BN>::kThreads, 1)
             }
 #pragma unroll
             for (int j = 0; j < kG; ++j)
-              vw[a][r][j] = __ldg(src + static_cast<int64_t>(kbc[j]) * (BROW ? p.N : 1));
+              vw[a][r][j] = __ldca(src + static_cast<int64_t>(kbc[j]) * (BROW ? p.N : 1));
           }
         }
         const bool ok = mbar_wait(&sfempty[slot], ((gi / C::kSFSlots) & 1u) ^ 1u, abort_flag);

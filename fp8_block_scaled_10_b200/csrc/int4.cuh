@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint4 xn[4];
   auto load_x = [&]() {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) xn[j] = __ldg(reinterpret_cast<const uint4*>(xp + 32 * j));
+    for (int j = 0; j < 4; ++j) xn[j] = __ldca(reinterpret_cast<const uint4*>(xp + 32 * j));
   };
   if (!C::kShareX) load_x();
   uint32_t mask = 0x000F000Fu, exponent = 0x43004300u;
@@ -563,9 +563,9 @@ __global__ void __launch_bounds__(256)
        o += static_cast<int64_t>(gridDim.x) * 256) {
     const int64_t i = o / kHalves;
     // the upper four channels are nibbles 2, 3 and 6, 7
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(q) + word_place(i)) >>
+    const uint32_t w = __ldca(reinterpret_cast<const uint32_t*>(q) + word_place(i)) >>
                        (8 * static_cast<int>(o % kHalves));
-    const float sc = __ldg(s + ((8 * i) >> lg));
+    const float sc = __ldca(s + ((8 * i) >> lg));
     float v[kV];
 #pragma unroll
     for (int e = 0; e < kV; ++e)

@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     auto load_scales = [&](int s) {
 #pragma unroll
       for (int q = 0; q < 2 * kGroups; ++q)
-        next[q] = 2 * kGroups * s + q < groups ? __ldg(sp + 2 * kGroups * s + q) : 0.0f;
+        next[q] = 2 * kGroups * s + q < groups ? __ldca(sp + 2 * kGroups * s + q) : 0.0f;
     };
     load_scales(0);
     for (int s = 0; s < steps; ++s) {

@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kStaticThreads)
         const uint32_t row = div_invariant(c, row_div);
         const uint32_t col = (c - row * chunks_per_row) * E;
         load_n<E>(x + static_cast<int64_t>(c) * E, v[u]);
-        sc[u] = __ldg(s + static_cast<int64_t>(row) * s_row_stride + (col >> lb));
+        sc[u] = __ldca(s + static_cast<int64_t>(row) * s_row_stride + (col >> lb));
       }
     }
 #pragma unroll
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kDeqThreads)
         const uint32_t col = (c - row * chunks_per_row) * 16;
         off[u] = static_cast<int64_t>(c) * 16;
         raw[u] = __ldcs(reinterpret_cast<const uint4*>(q + off[u]));
-        sc[u] = __ldg(s + static_cast<int64_t>(row >> row_shift) * s_row_stride + (col >> lb));
+        sc[u] = __ldca(s + static_cast<int64_t>(row >> row_shift) * s_row_stride + (col >> lb));
       } else {
         off[u] = -1;
       }
@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(kDeqThreads)
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kDeqThreads + threadIdx.x; i < total;
        i += static_cast<int64_t>(gridDim.x) * kDeqThreads) {
     const int64_t row = i / N, col = i - row * N;
-    const float v = e4m3_value(q[i]) * __ldg(s + (row >> row_shift) * s_row_stride + (col >> lb));
+    const float v = e4m3_value(__ldca(q + i)) * __ldca(s + (row >> row_shift) * s_row_stride + (col >> lb));
     if (OUT_BF16)
       static_cast<__nv_bfloat16*>(y)[i] = __float2bfloat16_rn(v);
     else
@@ -491,11 +491,11 @@ template <typename T>
 __device__ __forceinline__ float load_elem(const T* p);
 template <>
 __device__ __forceinline__ float load_elem<float>(const float* p) {
-  return *p;
+  return __ldca(p);
 }
 template <>
 __device__ __forceinline__ float load_elem<__nv_bfloat16>(const __nv_bfloat16* p) {
-  return __bfloat162float(*p);
+  return __bfloat162float(__ldca(p));
 }
 
 template <typename T>
@@ -622,7 +622,8 @@ __global__ void __launch_bounds__(256)
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < MN;
        i += static_cast<int64_t>(gridDim.x) * 256) {
     float acc = 0.0f;
-    for (int sp = 0; sp < splits; ++sp) acc += ws[sp * MN + i];
+#pragma unroll 4
+    for (int sp = 0; sp < splits; ++sp) acc += __ldcg(ws + sp * MN + i);
     if constexpr (std::is_same_v<OutT, float>)
       y[i] = acc;
     else

@@ -35,6 +35,11 @@ __device__ __forceinline__ uint64_t global_timer_ns() {
 // are visible, so it precedes every read of inputs another kernel may write.
 // pdl_trigger() lets the next such kernel start its own prologue early.
 // Without a programmatic dependency both return at once.
+// What another kernel may have written is read by coherent loads behind
+// pdl_wait() (__ldca, __ldcg, __ldcs, TMA, cp.async).  The non-coherent path
+// (ld.global.nc) requires data that is read-only while the kernel is resident,
+// and a kernel is resident from its launch, when the producer may still write and
+// an earlier reader on the same SM may still fill the L1 with the old values.
 __device__ __forceinline__ void pdl_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }

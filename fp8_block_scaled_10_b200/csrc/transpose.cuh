@@ -57,7 +57,7 @@ constexpr int kTrSmemBytes = 128 * kTrApitch * 4 + 128 * 32 * 4;
 
 __device__ __forceinline__ uint32_t tr_key(uint32_t j) { return ((j >> 2) ^ j) & 31u; }
 
-__global__ void __launch_bounds__(kTrThreads)
+__global__ void __launch_bounds__(kTrThreads, 4)
     fp8_transpose_kernel(const uint8_t* __restrict__ q, const float* __restrict__ s,
                          uint8_t* __restrict__ qt, float* __restrict__ st, int64_t R, int64_t C,
                          int64_t sr, int64_t sc) {
@@ -67,10 +67,11 @@ __global__ void __launch_bounds__(kTrThreads)
   __shared__ __align__(16) uint32_t smT[128 * 32];
   const int t = threadIdx.x;
   // block scales: sT[j][i] = s[i][j]
+#pragma unroll 1
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kTrThreads + t; i < sr * sc;
        i += static_cast<int64_t>(gridDim.x) * kTrThreads) {
     const int64_t a = i / sc, b = i - a * sc;
-    st[b * sr + a] = s[i];
+    st[b * sr + a] = __ldca(s + i);
   }
   const int64_t tiles_r = (R + 127) / 128, tiles_c = (C + 127) / 128;
   const int64_t ntiles = tiles_r * tiles_c;
@@ -147,11 +148,11 @@ __global__ void __launch_bounds__(256)
   const int64_t stride = static_cast<int64_t>(gridDim.x) * 256;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < sr * sc; i += stride) {
     const int64_t a = i / sc, b = i - a * sc;
-    st[b * sr + a] = s[i];
+    st[b * sr + a] = __ldca(s + i);
   }
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < R * C; i += stride) {
     const int64_t j = i / R, r = i - j * R;   // output element (j, r) = input (r, j)
-    qt[i] = q[r * C + j];
+    qt[i] = __ldca(q + r * C + j);
   }
 }
 
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(256)
     const int64_t r0 = (ti / ntc) * 32, c0 = (ti % ntc) * 32;
     for (int k = ty; k < 32; k += 8) {
       const int64_t r = r0 + k, c = c0 + tx;
-      tile[k][tx] = (r < rows && c < kbn) ? in[r * kbn + c] : 0.0f;
+      tile[k][tx] = (r < rows && c < kbn) ? __ldca(in + r * kbn + c) : 0.0f;
     }
     __syncthreads();
     for (int k = ty; k < 32; k += 8) {
