@@ -396,14 +396,6 @@ cudaError_t launch_quant_int4(const T* w, uint8_t* q, float* s, int64_t words, i
 // ---------------------------------------------------------------------------
 // Gradient norm and clipping
 // ---------------------------------------------------------------------------
-int clip_launches(int64_t n) { return static_cast<int>((n + clip::kMaxTensors - 1) / clip::kMaxTensors); }
-
-// CTAs of each norm launch: two per SM, fewer when many launches share the
-// partials' limit.
-int clip_partials(int64_t n, int sms) {
-  return std::max(1, std::min(2 * sms, clip::kMaxPartials / std::max(1, clip_launches(n))));
-}
-
 struct Range {
   uintptr_t lo, hi;
   int64_t index;
@@ -483,27 +475,24 @@ void fill_table(clip::Table* t, const void* const* grads, void* const* outs, con
   t->first[t->count] = chunks;
 }
 
-// Launches the partial sums; *partials receives their number.
+// Launches the partial sums; *partials receives the number of their slots.
 fp8bs_status run_norm_partials(const void* const* grads, const int64_t* numel,
                                const fp8bs_dtype* dtypes, int64_t n, double* ws, int sms,
                                cudaStream_t st, int* partials) {
   *partials = 0;
-  const int most = clip_partials(n, sms);
   for (int64_t i = 0; i < n; i += clip::kMaxTensors) {
     clip::Table t;
     fill_table(&t, grads, nullptr, numel, dtypes, nullptr, i, std::min<int64_t>(n, i + clip::kMaxTensors));
     if (t.first[t.count] == 0) continue;
-    const int grid = std::min(most, t.first[t.count]);
-    const cudaError_t e = launch(clip::norm_partial_kernel, grid, clip::kThreads, 0, st, t, ws + *partials);
+    const int grid = clip::launch_ctas(t.first[t.count], sms);
+    const cudaError_t e = launch(clip::norm_partial_kernel, grid, clip::kThreads, 0, st, t, ws, *partials);
     if (e != cudaSuccess) return cuda_fail(e, "grad_norm launch");
-    *partials += grid;
+    *partials = std::max(*partials, grid);
   }
   return FP8BS_OK;
 }
 
-size_t norm_workspace(int64_t n, int sms) {
-  return sizeof(double) * static_cast<size_t>(clip_partials(n, sms)) * std::max(1, clip_launches(n));
-}
+size_t norm_workspace(int sms) { return sizeof(double) * static_cast<size_t>(clip::max_ctas(sms)); }
 
 }  // namespace
 }  // namespace fp8bs
@@ -787,7 +776,7 @@ size_t fp8bs_grad_norm_workspace_size(int64_t n) {
   int dev;
   DeviceInfo* info;
   if (device_setup(&dev, &info) != FP8BS_OK) return 0;
-  return norm_workspace(n, info->sms);
+  return norm_workspace(info->sms);
 }
 
 fp8bs_status fp8bs_grad_norm(const void *const *grads, const int64_t* numel,
@@ -800,10 +789,10 @@ fp8bs_status fp8bs_grad_norm(const void *const *grads, const int64_t* numel,
   int dev;
   DeviceInfo* info;
   if ((r = device_setup(&dev, &info)) != FP8BS_OK) return r;
-  if (n > 0 && (!workspace || workspace_bytes < norm_workspace(n, info->sms) ||
+  if (n > 0 && (!workspace || workspace_bytes < norm_workspace(info->sms) ||
                 (reinterpret_cast<uintptr_t>(workspace) & 7u)))
     return fail(FP8BS_ERR_WORKSPACE, "workspace of %zu bytes (8-byte aligned) required",
-                norm_workspace(n, info->sms));
+                norm_workspace(info->sms));
   int partials = 0;
   double* ws = static_cast<double*>(workspace);
   if ((r = run_norm_partials(grads, numel, dtypes, n, ws, info->sms, as_stream(stream), &partials)) != FP8BS_OK)
@@ -830,10 +819,10 @@ fp8bs_status fp8bs_clip_grads(const void *const *grads, void *const *outs, const
   int dev;
   DeviceInfo* info;
   if ((r = device_setup(&dev, &info)) != FP8BS_OK) return r;
-  if (n > 0 && (!workspace || workspace_bytes < norm_workspace(n, info->sms) ||
+  if (n > 0 && (!workspace || workspace_bytes < norm_workspace(info->sms) ||
                 (reinterpret_cast<uintptr_t>(workspace) & 7u)))
     return fail(FP8BS_ERR_WORKSPACE, "workspace of %zu bytes (8-byte aligned) required",
-                norm_workspace(n, info->sms));
+                norm_workspace(info->sms));
   cudaStream_t stm = as_stream(stream);
   int partials = 0;
   double* ws = static_cast<double*>(workspace);
@@ -851,7 +840,7 @@ fp8bs_status fp8bs_clip_grads(const void *const *grads, void *const *outs, const
     clip::Table t;
     fill_table(&t, grads, outs, numel, dtypes, out_dtypes, i, std::min<int64_t>(n, i + clip::kMaxTensors));
     if (t.first[t.count] == 0) continue;
-    const int grid = std::min(2 * info->sms, t.first[t.count]);
+    const int grid = clip::launch_ctas(t.first[t.count], info->sms);
     e = launch(clip::clip_scale_kernel, grid, clip::kThreads, 0, stm, t, static_cast<const double*>(ws),
                partials, *max_norm, norm_out);
     if (e != cudaSuccess) return cuda_fail(e, "clip_grads launch");
