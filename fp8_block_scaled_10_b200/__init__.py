@@ -927,7 +927,8 @@ def clip_grads(grads, max_norm, out=None):
     out: None (in place; nothing is written when nothing is clipped) or a list of
     bfloat16 or float32 tensors of the gradients' shapes that receive the
     scaled values.  Outputs may not overlap one another nor another tensor's
-    gradient.  A NaN norm makes every output NaN, an infinite one scales by 0."""
+    gradient.  A NaN norm makes every output NaN, an infinite one scales by 0 (with
+    max_norm=inf too)."""
     ptrs, types = _grad_arrays(grads, "grads")
     n, dev = len(grads), grads[0].device
     if out is None:

@@ -187,8 +187,8 @@ __device__ __forceinline__ void scale_chunk(const TI* p, TO* o, int64_t n, float
   for (int64_t i = done + threadIdx.x; i < n; i += kThreads) store_one(o + i, load_one(p + i) * scale);
 }
 
-// A norm that is NaN scales by NaN, an infinite one by 0 (an infinite
-// gradient then becomes NaN): nothing that went wrong is passed on as a
+// A norm that is NaN scales by NaN, an infinite one by 0 whatever the bound (an
+// infinite gradient then becomes NaN): nothing that went wrong is passed on as a
 // plausible step.  In place and with nothing to clip, nothing is written:
 // times 1 is the value that stands there.
 __global__ void __launch_bounds__(kThreads)
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads)
   pdl_wait();
   const double v = norm_of(partials, n, smem);
   if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(v);
-  const double r = max_norm / (v + 1e-6);
+  const double r = isinf(v) ? 0.0 : max_norm / (v + 1e-6);
   const float scale = r >= 1.0 ? 1.0f : static_cast<float>(r);
   const int chunks = t.first[t.count];
   for (int c = chunks - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= gridDim.x) {

@@ -739,7 +739,7 @@ FP8BS_API fp8bs_status fp8bs_grad_norm(const void *const *grads, const int64_t *
  * clip_grads: out[i] = grad[i] * min(1, *max_norm / (norm + 1e-6)) for every
  * element of n tensors, with norm as for grad_norm (used in 64 bits; the
  * factor is rounded to fp32, the product once to the output's type).  A NaN norm
- * makes every output NaN; an infinite one scales by 0.
+ * makes every output NaN; an infinite one scales by 0, whatever max_norm is.
  *   outs, out_dtypes  HOST arrays: the outputs' device pointers and types.
  *            outs[i] may be grads[i] (same type: in place; nothing is written when
  *            nothing is clipped).  Any other overlap of an output with an output or
