@@ -427,26 +427,30 @@ fp8bs_status check_grads(const void* const* grads, const int64_t* numel, const f
 // read, the same element.  An output may be its own gradient.
 fp8bs_status check_outputs(const void* const* grads, void* const* outs, const int64_t* numel,
                            const fp8bs_dtype* dtypes, const fp8bs_dtype* out_dtypes, int64_t n) {
-  std::vector<Range> r;
-  r.reserve(static_cast<size_t>(n));
+  if (n == 0) return FP8BS_OK;
+  // (No exception may leave the C entry that this is called from.)
+  const std::unique_ptr<Range[]> ranges(new (std::nothrow) Range[static_cast<size_t>(n)]);
+  if (!ranges) return fail(FP8BS_ERR_WORKSPACE, "no host memory for the ranges of %lld outputs", (long long)n);
+  Range* const r = ranges.get();
+  Range* end = r;
   auto bytes = [](fp8bs_dtype t) { return t == FP8BS_DTYPE_BF16 ? 2 : 4; };
   for (int64_t i = 0; i < n; ++i) {
     if (numel[i] == 0) continue;
     const uintptr_t lo = reinterpret_cast<uintptr_t>(outs[i]);
-    r.push_back({lo, lo + static_cast<uintptr_t>(numel[i]) * bytes(out_dtypes[i]), i});
+    *end++ = {lo, lo + static_cast<uintptr_t>(numel[i]) * bytes(out_dtypes[i]), i};
   }
-  std::sort(r.begin(), r.end());
-  for (size_t i = 1; i < r.size(); ++i)
-    if (r[i].lo < r[i - 1].hi)
-      return fail(FP8BS_ERR_INVALID_ARG, "outputs %lld and %lld overlap", (long long)r[i - 1].index,
-                  (long long)r[i].index);
+  std::sort(r, end);
+  for (const Range* o = r + 1; o < end; ++o)
+    if (o->lo < o[-1].hi)
+      return fail(FP8BS_ERR_INVALID_ARG, "outputs %lld and %lld overlap", (long long)o[-1].index,
+                  (long long)o->index);
   for (int64_t i = 0; i < n; ++i) {
     if (numel[i] == 0) continue;
     const uintptr_t lo = reinterpret_cast<uintptr_t>(grads[i]);
     const uintptr_t hi = lo + static_cast<uintptr_t>(numel[i]) * bytes(dtypes[i]);
-    auto it = std::upper_bound(r.begin(), r.end(), Range{lo, 0, 0});
-    if (it != r.begin()) --it;
-    for (; it != r.end() && it->lo < hi; ++it) {
+    const Range* it = std::upper_bound(r, end, Range{lo, 0, 0});
+    if (it != r) --it;
+    for (; it != end && it->lo < hi; ++it) {
       if (it->hi <= lo) continue;
       if (it->index == i && outs[i] == grads[i] && out_dtypes[i] == dtypes[i]) continue;
       return fail(FP8BS_ERR_INVALID_ARG, "output %lld overlaps gradient %lld", (long long)it->index,

@@ -16,8 +16,9 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <memory>
 #include <mutex>
-#include <vector>
+#include <new>
 
 #include "clip.cuh"
 #include "fp8bs.h"

@@ -64,7 +64,8 @@ typedef enum fp8bs_status {
     FP8BS_OK = 0,
     FP8BS_ERR_INVALID_ARG = 1, /* bad pointer, size, alignment or shape; nothing launched */
     FP8BS_ERR_UNSUPPORTED = 2, /* well-formed but not implemented (e.g. block = 48)      */
-    FP8BS_ERR_WORKSPACE = 3,   /* workspace missing or smaller than *_workspace_size()   */
+    FP8BS_ERR_WORKSPACE = 3,   /* workspace missing or smaller than *_workspace_size(),
+                                  or no host memory for a call's checks             */
     FP8BS_ERR_CUDA = 4,        /* a CUDA runtime/driver call failed                      */
     FP8BS_ERR_TIMEOUT = 5,     /* a device-side bounded wait gave up (device error word) */
     FP8BS_ERR_SCALE = 6        /* a *_ue8m0 GEMM met a scale that is not a positive normal
