@@ -212,61 +212,31 @@ struct Int4Launch {
   }
 };
 
-// Clusters of each size that the GPU holds at once for one kernel: fewer than
-// SMs / size where a size does not divide the SMs of a GPC.  Asked once per
-// device and kernel.
-struct ClusterSlots {
-  std::atomic<int> n[kMaxDevices][9] = {};
-  template <typename Kernel>
-  int operator()(Kernel* kernel, const Int4Launch& like, int dev, int size) {
-    int v = n[dev][size].load(std::memory_order_relaxed);
-    if (v == 0) {
-      Int4Launch l = like;
-      l.cfg.attrs = l.attr;
-      l.grid(1, size, 1);
-      if (cudaOccupancyMaxActiveClusters(&v, kernel, &l.cfg) != cudaSuccess || v < 1) {
-        (void)cudaGetLastError();
-        v = 1;
-      }
-      n[dev][size].store(v, std::memory_order_relaxed);
-    }
-    return v;
-  }
-};
-
-// CTAs of a cluster that share the channels of a row block: the number that
-// gives the least time, counted in 128-channel blocks of a warp (or CTA): rounds
-// of the GPU's clusters times a share of the blocks, a fixed cost per round and,
-// from two CTAs on, one for the join.
-template <typename Slots>
-int int4_splits(int64_t units, int kblocks, int warps_k, int fixed, int join, Slots slots) {
-  int best = 1;
-  int64_t best_cost = -1;
-  for (int s = 1; s <= 8 && (s == 1 || s * warps_k <= kblocks); ++s) {
-    const int64_t at_once = slots(s);
-    const int64_t rounds = (units + at_once - 1) / at_once;
-    const int64_t cost =
-        rounds * ((kblocks + s * warps_k - 1) / (s * warps_k) + fixed + (s > 1 ? join : 0));
-    if (best_cost < 0 || cost < best_cost) {
-      best = s;
-      best_cost = cost;
-    }
-  }
-  return best;
+// The runtime's answer for one kernel: clusters of `size` CTAs that the GPU holds at once.
+template <typename Kernel>
+auto cluster_query(Kernel* kernel, const Int4Launch& like) {
+  return [kernel, &like](int size, int* clusters) {
+    Int4Launch l = like;
+    l.cfg.attrs = l.attr;
+    l.grid(1, size, 1);
+    return cudaOccupancyMaxActiveClusters(clusters, kernel, &l.cfg);
+  };
 }
 
 template <int NT, int G, bool GATED>
 cudaError_t launch_int4(const w4::Params& p, int dev, cudaStream_t st) {
   using C = w4::Cfg<NT, G, GATED>;
-  static ClusterSlots slots;
+  static ClusterSlots<kMaxDevices> slots;
   auto kernel = w4::int4_linear_kernel<NT, G, GATED>;
   Int4Launch l(w4::kThreads, C::kSmem, st);
-  auto at_once = [&](int s) { return slots(kernel, l, dev, s); };
   const int64_t blocks = (p.N + C::kRows - 1) / C::kRows;
   // Measured: a join costs about 3 blocks of a warp, with or without a cluster.
-  const int splits = int4_splits(blocks, p.K / 128, C::WK, 3, 0, at_once);
+  ClusterChoice c;
+  const cudaError_t e =
+      choose_cluster(blocks, p.K / 128, C::WK, 3, 0, slots.of(dev), cluster_query(kernel, l), &c);
+  if (e != cudaSuccess) return e;
   // A cluster walks several row blocks where there are more than fit.
-  l.grid(std::min<int64_t>(blocks, at_once(splits)), splits, 1);
+  l.grid(std::min<int64_t>(blocks, c.at_once), c.size, 1);
   return cudaLaunchKernelEx(&l.cfg, kernel, p);
 }
 
@@ -274,7 +244,7 @@ cudaError_t launch_int4(const w4::Params& p, int dev, cudaStream_t st) {
 template <int G, bool GATED>
 cudaError_t launch_int4_tile(const CUtensorMap& q0, const CUtensorMap& q1, const CUtensorMap& x,
                              const w4::Params& p, int dev, cudaStream_t st) {
-  static ClusterSlots slots;
+  static ClusterSlots<kMaxDevices> slots;
   auto kernel = w4::int4_tile_kernel<G, GATED>;
   Int4Launch l(w4::kTileThreads, w4::kTileSmem, st);
   const int rows = GATED ? 64 : 128;
@@ -282,9 +252,11 @@ cudaError_t launch_int4_tile(const CUtensorMap& q0, const CUtensorMap& q1, const
   const int64_t passes = (p.M + w4::kTok - 1) / w4::kTok;
   // Measured: a CTA's start and end cost 12 of its blocks (0.45 us each), a
   // cluster's join 6 more.
-  const int splits = int4_splits(tiles * passes, p.K / 128, 1, 12, 6,
-                                 [&](int s) { return slots(kernel, l, dev, s); });
-  l.grid(tiles, splits, passes);
+  ClusterChoice c;
+  const cudaError_t e =
+      choose_cluster(tiles * passes, p.K / 128, 1, 12, 6, slots.of(dev), cluster_query(kernel, l), &c);
+  if (e != cudaSuccess) return e;
+  l.grid(tiles, c.size, passes);
   return cudaLaunchKernelEx(&l.cfg, kernel, q0, q1, x, p);
 }
 

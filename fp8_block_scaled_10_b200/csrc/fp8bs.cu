@@ -11,7 +11,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -21,6 +20,7 @@
 #include <new>
 
 #include "clip.cuh"
+#include "clusters.h"
 #include "fp8bs.h"
 #include "gated.cuh"
 #include "gemm.cuh"
