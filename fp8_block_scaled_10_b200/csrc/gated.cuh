@@ -163,8 +163,8 @@ __device__ __forceinline__ NegGateGrad2 neg_gate_grad2(float2 g, float2 u, float
 // in the place of x - q s.  The estimate is off by two ulps at most, so the step
 // leaves an error of 2^-22 ulp before its rounding: the result is the correctly
 // rounded quotient unless x / s lies that near to the middle of two fp32 numbers,
-// and then one of the two.  (The values come from an approximate sigmoid, 2^-22
-// off themselves; the second step would change nothing but the time, 233 us
+// and then one of the two.  (The values come from an approximate sigmoid, 2^-21
+// off themselves or more; the second step would change nothing but the time, 233 us
 // instead of 204 at [4096, 18432], where fp32 operations are what binds.)
 // With these signs a zero keeps its sign (-0: 0 * nr = -0, the residual -0 + 0 = 0,
 // and 0 nr + -0 = -0), so there is none to put back.  s is 0 where the scale is

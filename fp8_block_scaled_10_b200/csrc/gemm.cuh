@@ -397,10 +397,12 @@ __host__ __device__ __forceinline__ Unit grouped_unit(const Params& p, const int
   return t;
 }
 
-// Sigmoid and SiLU in fp32: 1 / (1 + 2^(-x log2 e)) from the hardware's exp2 and
-// reciprocal, a few 2^-22 relative, below every output format's rounding (bf16
-// 2^-8) and below the accumulation's own error.  2^y overflowing to infinity
-// gives 0; a subnormal 2^y, flushed to 0, is lost against the 1 anyway.
+// Sigmoid and SiLU in fp32 for bf16 and FP8 outputs: 1 / (1 + 2^(-x log2 e)) from the
+// hardware's exp2 and reciprocal.  x log2 e is rounded before the exponential, so
+// the relative error grows with |x| for negative x: (1.25 |x| + 8) 2^-24 at most,
+// 2^-21 near 0 and 2^-17 at -87, under the outputs' half steps (bf16 2^-8, e4m3
+// 2^-4).  Below -87.3, where the sigmoid is under 2^-126, 2^y overflows or the
+// reciprocal flushes, and it is 0.  (fp32 outputs take int4.cuh's gated_wide.)
 __device__ __forceinline__ float exp2_ftz(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
