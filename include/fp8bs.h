@@ -647,7 +647,9 @@ FP8BS_API fp8bs_status fp8bs_fp8_gemm_grouped_gated(int64_t G, const int64_t *m_
  *   dgu    device, [M, 2N] bf16, written: dg in columns 0 .. N-1, du behind
  *   h      device, [M, N] bf16, or NULL: the block's h again (the operand of the
  *          down projection's weight gradient), so that it need not be kept
- * The outputs must not overlap the inputs.  M == 0 or N == 0 is a no-op.
+ * All tensors are aligned to their 2-byte elements (with N % 8 == 0 and 16-byte
+ * alignment they are read and written 16 bytes at a time).  The outputs must not overlap
+ * the inputs.  M == 0 or N == 0 is a no-op.
  */
 FP8BS_API fp8bs_status fp8bs_gated_backward(const uint16_t *gu, const uint16_t *dh, int64_t M,
                                             int64_t N, uint16_t *dgu, uint16_t *h, void *stream);
