@@ -564,7 +564,9 @@ __global__ void __launch_bounds__(256)
 // y = (c - 8) s: the fp32 product, rounded to bf16 or stored.  A thread stores
 // 16 bytes: a word's 8 channels in bf16, half of them in fp32.  Bound by the
 // stores ([18432, 7168]: bf16 60 us, 5.6 TB/s; fp32 111 us, 5.5 TB/s, 150 us with
-// 32 bytes per thread).
+// 32 bytes per thread).  In bf16 the loads of two words are in flight before the
+// first store, which no later load passes (one word: 65 us); in fp32, with half the
+// loads per byte stored, two took 112.
 template <typename T>
 __global__ void __launch_bounds__(256)
     dequant_int4_kernel(const uint8_t* __restrict__ q, const float* __restrict__ s,
@@ -572,24 +574,40 @@ __global__ void __launch_bounds__(256)
   pdl_trigger();
   pdl_wait();
   constexpr int kHalves = static_cast<int>(sizeof(T)) / 2, kV = 8 / kHalves;
-  for (int64_t o = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; o < kHalves * nwords;
-       o += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t i = o / kHalves;
-    // the upper four channels are nibbles 2, 3 and 6, 7
-    const uint32_t w = __ldca(reinterpret_cast<const uint32_t*>(q) + word_place(i)) >>
-                       (8 * static_cast<int>(o % kHalves));
-    const float sc = __ldca(s + ((8 * i) >> lg));
-    float v[kV];
+  constexpr int kDequantWords = 2 / kHalves;
+  const int64_t items = kHalves * nwords, step = static_cast<int64_t>(gridDim.x) * 256;
+  for (int64_t first = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; first < items;
+       first += kDequantWords * step) {
+    uint32_t w[kDequantWords];
+    float sc[kDequantWords];
 #pragma unroll
-    for (int e = 0; e < kV; ++e)
-      v[e] = static_cast<float>(static_cast<int>((w >> (4 * (e / 2 + 4 * (e & 1)))) & 15u) - 8) * sc;
-    if constexpr (sizeof(T) == 2) {
-      uint32_t h[4];
+    for (int u = 0; u < kDequantWords; ++u) {
+      const int64_t o = first + u * step, i = o / kHalves;
+      w[u] = 0;
+      sc[u] = 0.0f;
+      if (o < items) {
+        // the upper four channels are nibbles 2, 3 and 6, 7
+        w[u] = __ldca(reinterpret_cast<const uint32_t*>(q) + word_place(i)) >>
+               (8 * static_cast<int>(o % kHalves));
+        sc[u] = __ldca(s + ((8 * i) >> lg));
+      }
+    }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) h[e] = gemm::pack_bf16x2(v[2 * e], v[2 * e + 1]);
-      __stcs(reinterpret_cast<uint4*>(y + 8 * o), make_uint4(h[0], h[1], h[2], h[3]));
-    } else {
-      __stcs(reinterpret_cast<float4*>(y + 4 * o), make_float4(v[0], v[1], v[2], v[3]));
+    for (int u = 0; u < kDequantWords; ++u) {
+      const int64_t o = first + u * step;
+      if (o >= items) break;
+      float v[kV];
+#pragma unroll
+      for (int e = 0; e < kV; ++e)
+        v[e] = static_cast<float>(static_cast<int>((w[u] >> (4 * (e / 2 + 4 * (e & 1)))) & 15u) - 8) * sc[u];
+      if constexpr (sizeof(T) == 2) {
+        uint32_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[e] = gemm::pack_bf16x2(v[2 * e], v[2 * e + 1]);
+        __stcs(reinterpret_cast<uint4*>(y + 8 * o), make_uint4(h[0], h[1], h[2], h[3]));
+      } else {
+        __stcs(reinterpret_cast<float4*>(y + 4 * o), make_float4(v[0], v[1], v[2], v[3]));
+      }
     }
   }
 }
