@@ -616,7 +616,8 @@ def fp8_gemm_gated(a, a_s, w_gate, w_gate_s, w_up, w_up_s, return_gu=False):
 
     a: [..., K] e4m3fn, a_s: [..., K/128] float32 (act_quant's output),
     w_gate, w_up: [N, K] e4m3fn, their scales [cdiv(N,128), K/128] float32 (any
-    positive scales; powers of two need no flag) -> h: [..., N] bfloat16.  With
+    positive scales; powers of two take the same kernel, not the block-scaled MMA of
+    fp8_gemm's scale_fmt="ue8m0") -> h: [..., N] bfloat16.  With
     return_gu also the bfloat16 pre-activations [..., 2N], gate first, which
     gated_backward takes."""
     M, N, K = _gated_operands(a, a_s, w_gate, w_gate_s, w_up, w_up_s)
@@ -653,7 +654,9 @@ def fp8_gemm_gated_quant(a, a_s, w_gate, w_gate_s, w_up, w_up_s, out_scale_fmt=N
 
 @_on_device
 def fp8_gemm_grouped_gated(a, a_s, w_gate, w_gate_s, w_up, w_up_s, m_offsets):
-    """fp8_gemm_gated per expert, over rows grouped contiguously by expert.
+    """fp8_gemm_gated per expert, over rows grouped contiguously by expert (h
+    alone: the pre-activations that gated_backward takes come from two
+    fp8_gemm_grouped calls).
 
     a: [M_total, K] e4m3fn, a_s: [M_total, K/128], w_gate, w_up: [G, N, K], their
     scales [G, cdiv(N,128), K/128], m_offsets: [G+1] int64 on the device ->
@@ -845,8 +848,9 @@ def _int4_tokens(x, K, out_dtype):
 
 @_on_device
 def int4_linear(x, q, s, out_dtype=torch.bfloat16):
-    """y = x @ W^T on a packed 4-bit weight, for decode-sized token counts (the
-    weight is read once per 32 tokens).
+    """y = x @ W^T on a packed 4-bit weight, for decode-sized token counts: the
+    weight is read and expanded once per 32 tokens, so that from about 128 tokens on
+    weight_dequant_int4 and a bf16 product take less time.
 
     x: [..., K] bfloat16, q: uint8 [N, K/2], s: float32 [N, K/group] (as
     weight_quant_int4 returns them) -> y: [..., N] bfloat16 or float32."""

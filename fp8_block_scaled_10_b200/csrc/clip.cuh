@@ -5,8 +5,8 @@
 // one order, so the norm has the same bits every time) and scales.  Both are
 // streams over the tensors cut into chunks; the second pass walks the chunks
 // from the last one back, so that what the first pass left in the L2 is read
-// there.  The norm alone: 64 x [7168, 2048] fp32 (3.8 GB) in 598 us, 6.3 TB/s.
-// Clipping 396 M fp32 gradients (1.59 GB read twice and written once): 748 us, 6.4
+// there.  The norm alone: 64 x [7168, 2048] fp32 (3.8 GB) in 624 us, 6.0 TB/s.
+// Clipping 396 M fp32 gradients (1.59 GB read twice and written once): 751 us, 6.3
 // TB/s.  40 tensors, 600 thousand elements: 10 us, two launches' latency.
 #pragma once
 

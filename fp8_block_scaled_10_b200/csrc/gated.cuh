@@ -179,8 +179,8 @@ __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 
 
 // bf16 gu [M, 2N] (gate columns first), dh [M, N] -> dgu [M, 2N] and, unless
 // h is null, h [M, N].  A stream of 6 bytes in and 4 or 6 out per element: eight
-// columns per thread where N % 8 == 0 (all 16-byte aligned).  [4096, 18432]: 116 us
-// without h, 147 with it, 6.5 and 6.2 TB/s.
+// columns per thread where N % 8 == 0 and all tensors are 16-byte aligned.  [4096,
+// 18432]: 116 us without h, 148 with it, 6.5 and 6.1 TB/s.
 __global__ void __launch_bounds__(256)
     gated_backward_kernel(const __nv_bfloat16* __restrict__ gu, const __nv_bfloat16* __restrict__ dh,
                           __nv_bfloat16* __restrict__ dgu, __nv_bfloat16* __restrict__ h, int64_t M,
@@ -216,12 +216,13 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// The same for any N and alignment: a CTA takes 2048 columns of a row, eight per thread, 256
-// columns apart (2-byte accesses along the row, all loads before the first use;
-// the row and column are the CTA's, so there is no division per element).
+// The same for any N and alignment: a CTA takes 2048 columns of a row, eight per
+// thread, 256 columns apart (2-byte accesses along the row, all loads before the
+// first use; the row and column are the CTA's, so there is no division per element).
 // The loads stay in L1: neighbouring warps share the sectors at their ends (streaming
 // loads: 209 and 274 us).
-// [4096, 18431]: 164 us without h, 211 with it.
+// [4096, 18431]: 163 us without h, 207 with it; bound by the accesses, four times as
+// many as the wide kernel's per byte.
 constexpr int kAnyCols = 8 * 256;
 __global__ void __launch_bounds__(256)
     gated_backward_any_kernel(const __nv_bfloat16* __restrict__ gu,

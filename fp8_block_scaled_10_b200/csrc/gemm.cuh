@@ -614,9 +614,9 @@ __device__ __forceinline__ bool gated_store(const Params& p, const Unit& t, floa
 // unless it is asked for (p.gu).  Everything up to the epilogue's stores is
 // the dense kernel's, and so are its bounds (the tensor core and the FP32
 // promotion at prefill sizes, the weight stream at decode sizes).
-// Measured: 4096 tokens, 7168 -> 2 x 18432 with gu 1028 us (2106 TFLOP/s; 5-6 %
+// Measured: 4096 tokens, 7168 -> 2 x 18432 with gu 1043 us (2076 TFLOP/s; 5-6 %
 // slower than the dense GEMM of the same size without gu, 11 % with it); 32
-// experts, 16384 rows, 7168 -> 2 x 2048: 577 us (1667 TFLOP/s).
+// experts, 16384 rows, 7168 -> 2 x 2048: 583 us (1650 TFLOP/s).
 template <int BN, bool GROUPED, int ARows = 128, bool BROW = false, bool CHECK = false,
           bool FUSED = false, bool GATED = false>
 __global__ void __launch_bounds__(Cfg<BN, ARows>::kThreads, 1)

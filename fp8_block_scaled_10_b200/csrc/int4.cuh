@@ -199,8 +199,8 @@ __device__ __forceinline__ void group_sync(int id) {
 // memory and a product costs the same for 1 token as for 32; measured at 16
 // tokens, this kernel against that: 7168 -> 18432 24.4 / 30.6 us, 18432 -> 7168
 // 26.1 / 38.7, gated 7168 -> 2048 10.4 / 11.7; at 32, in two passes' worth of
-// tiles, 41.4 / 40.0 and 17.3 / 12.2.)
-// One token, 7168 -> 18432 (70 MB): 17.7 us, 4.0 TB/s; 55 % of the
+// tiles, 41.4 / 40.2 and 17.3 / 12.2.)
+// One token, 7168 -> 18432 (70 MB): 17.8 us, 3.9 TB/s; 55 % of the
 // issue slots are taken, and 43 % of the instructions are the integer pipe's, which
 // expands the codes at half rate; the rest is the start and the join of a kernel
 // this short.

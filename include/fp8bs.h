@@ -549,8 +549,10 @@ FP8BS_API fp8bs_status fp8bs_fp8_gemm_quant(const uint8_t *a, const float *a_s, 
  *
  * fp8_gemm_gated: both projections, the activation and the product in one
  * kernel, on block-scaled FP8 operands with FP32 accumulation (each operand
- * and scale as for fp8bs_fp8_gemm, any positive fp32 scales, powers of two
- * among them):
+ * and scale as for fp8bs_fp8_gemm, any positive fp32 scales; powers of two take the
+ * same kernel, and at prompt sizes two fp8bs_fp8_gemm_ue8m0 calls with an elementwise
+ * gate behind them are 5-6 % faster for those: 928 against 988 us at 4096 tokens, 7168
+ * -> 18432):
  *   g[m, n] = sum_kb a_s[m, kb] w_gate_s[n / 128, kb] P_kb[m, n],  u likewise,
  *   h[m, n] = bf16(g sigmoid(g) u)     (one rounding)
  * The gate is computed in fp32 with a fast sigmoid: g sigmoid(g) u is off by
@@ -628,7 +630,9 @@ FP8BS_API fp8bs_status fp8bs_fp8_gated_ffn(const uint16_t *x, int64_t M, int64_t
  * fp8_gemm_grouped_gated: fp8_gemm_gated per expert over rows grouped
  * contiguously, with m_offsets, G, M_total and the weights' layouts
  * ([G, N, K], [G, cdiv(N, 128), K / 128]) as for fp8bs_fp8_gemm_grouped.  Rows of h
- * that belong to no group are left untouched.  Needs no workspace.
+ * that belong to no group are left untouched.  Needs no workspace.  There is no gu
+ * output: a backward pass per expert takes its pre-activations from two
+ * fp8bs_fp8_gemm_grouped calls.
  */
 FP8BS_API fp8bs_status fp8bs_fp8_gemm_grouped_gated(int64_t G, const int64_t *m_offsets,
                                                     int64_t M_total, const uint8_t *a,
@@ -710,7 +714,10 @@ FP8BS_API fp8bs_status fp8bs_weight_dequant_int4(const uint8_t *q, const float *
  *   q, s   device, as fp8bs_weight_quant_int4 writes them (s 16-byte aligned)
  *   y      device, [M, N], bf16 (y_dtype = BF16) or fp32, written
  * Up to 32 tokens read the weight once; more take a pass per 32 (any M up to
- * 524280).  Needs no workspace.  M == 0 or N == 0 is a no-op.
+ * 524280), each expanding the weight again: from about 128 tokens on
+ * fp8bs_weight_dequant_int4 and a bf16 GEMM take less time (7168 -> 18432: 60 us at
+ * 64 tokens, 118 against 115 at 128, 234 against 121 at 256, 3.6 ms against 0.7 at
+ * 4096).  Needs no workspace.  M == 0 or N == 0 is a no-op.
  */
 FP8BS_API fp8bs_status fp8bs_int4_linear(const uint16_t *x, int64_t M, const uint8_t *q,
                                          const float *s, int64_t N, int64_t K, int64_t group,
