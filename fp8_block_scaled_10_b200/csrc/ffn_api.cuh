@@ -634,7 +634,7 @@ fp8bs_status fp8bs_gated_backward(const uint16_t* gu, const uint16_t* dh, int64_
     if (reinterpret_cast<uintptr_t>(v) & 1u)
       return fail(FP8BS_ERR_INVALID_ARG, "operands must be aligned to their 2-byte elements");
   // 16-byte accesses where every row starts on 16 bytes (N % 8 == 0: all rows do if
-  // the tensors do), else 2-byte ones ([4096, 18432] with h: 147 and 184 us).
+  // the tensors do), else 2-byte ones ([4096, 18432] with h: 148 and 184 us).
   const bool wide = N % 8 == 0 && aligned16(gu) && aligned16(dh) && aligned16(dgu) && aligned16(h);
   int dev;
   DeviceInfo* info;

@@ -79,7 +79,7 @@ def test_split_partials_of_alternating_calls_in_one_workspace(M, N, K):
 @pytest.mark.parametrize("M", [1, 12, 32])
 def test_chains_over_the_same_buffers(M):
     """act_quant -> GEMM -> 4-bit gate -> 4-bit linear, every intermediate in one
-    buffer that the next round overwrites."""
+    buffer that the next pass overwrites."""
     g = _gen(50 + M)
     K, N, F = 1024, 1024, 512
     w, ws_ = _weight(g, N, K)
